@@ -165,12 +165,14 @@ cudaError_t launch_clip(int count, const void *const *in, void *const *out, cons
                         float max_norm, float *norm, double *part, cudaStream_t s);
 
 // ---- linear (linear.cu, linear_simt.cu) ----
-// The activations: value and slope.  The fp32 path calls the exact functions; the
-// bf16 path (FAST) the hardware exponential and, for the error function, the
-// rational approximation 7.1.26 of Abramowitz and Stegun, Handbook of
-// Mathematical Functions (absolute error 1.5e-7): far below half a step of bf16
-// (2^-8), at a third of the instructions.  Its e^(-z^2/2) is the one the slope
-// needs as well.
+// The activations: value and slope.  The fp32 path calls CUDA's functions, the
+// normal distribution as erfc (1 + erf cancels for negative z: 4 % off at z = -5).
+// The bf16 path (FAST) takes the hardware exponential and, for erfc, the rational
+// approximation 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// Functions, at a third of the instructions; its e^(-z^2/2) is the one the slope
+// needs as well.  Its error of 1.5e-7 is an absolute one: below half a step of
+// bf16 (2^-8 of the value) down to z = -6, where gelu is -6e-9, and 1 % of gelu's
+// -5e-15 at z = -8.
 // The exponential and the reciprocal flush denormals: what would be one rounds to
 // nothing beside the terms it is added to, and the handling costs more than both.
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -200,7 +202,7 @@ template <int ACT, bool FAST>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == KDA_ACT_SILU) return FAST ? z * sigmoid_fast(z) : z / (1.f + expf(-z));
   if constexpr (ACT == KDA_ACT_GELU)
-    return FAST ? z * normal_fast(z).x : 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    return FAST ? z * normal_fast(z).x : 0.5f * z * erfcf(z * -0.70710678118654752f);
   if constexpr (ACT == KDA_ACT_SIGMOID) return FAST ? sigmoid_fast(z) : 1.f / (1.f + expf(-z));
   return z;
 }
@@ -215,7 +217,7 @@ __device__ __forceinline__ float act_slope(float z) {
       const float2 n = normal_fast(z);
       return fmaf(z * 0.39894228040143268f, n.y, n.x);
     }
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    return 0.5f * erfcf(z * -0.70710678118654752f) + z * 0.39894228040143268f * expf(-0.5f * z * z);
   }
   if constexpr (ACT == KDA_ACT_SIGMOID) {
     // e / (1 + e)^2 with e = e^-|z|: p (1 - p) cancels for large z (17 % off at z = 15 in fp32, 0 from 17 on)

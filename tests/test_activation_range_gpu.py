@@ -3,7 +3,9 @@ their own size: the tails are small, and a term that cancels there loses them wh
 
 A layer of one input with weight 1 is its activation: y = act(z), and with dy = 1 its
 dx is the slope at the pre-activation.  Bounds count steps of fp32 (E32): expf is off
-by 2, an addition, product or quotient by half of one."""
+by 2, erfcf by 4, an addition, product or quotient by half of one."""
+import math
+
 import pytest
 import torch
 
@@ -31,13 +33,19 @@ def exact(z, act):
     dp = e / (1 + e) ** 2
     if act == "sigmoid":
         return p, dp, dp
-    return z * p, p + z * dp, p + (z * dp).abs()
+    if act == "silu":
+        return z * p, p + z * dp, p + (z * dp).abs()
+    c = 0.5 * torch.special.erfc(-z * math.sqrt(0.5))
+    d = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    return z * c, c + z * d, c + (z * d).abs()
 
 
 def steps(z, act, dtype):
     """Relative error of the value's and the slope's terms, in steps of fp32."""
     if dtype == BF16:
         return 32 + z.abs()  # the exponential's argument is rounded once: |z| / 2 of a step and the instruction's two
+    if act == "gelu":  # z / sqrt 2 is rounded twice, and the tail's exponent is z^2 / 2 of it
+        return 16 + 2 * z * z
     return 8 + z.abs() * (act == "silu")  # silu's 1 - p is a difference, times z
 
 
@@ -48,16 +56,18 @@ def close(name, got, ref, bound):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid"])
 def test_value_and_slope(act, dtype):
     z = points(dtype)
     one = torch.ones(1, 1, device="cuda", dtype=dtype)
     value, slope, size = exact(z.double(), act)
     n = steps(z.double(), act, dtype) * E32
+    # erfc's approximation in bf16 is 1.5e-7 off and 1 - erfc / 2 rounds once: absolute terms
+    lost = 0.75e-7 + E32 if act == "gelu" and dtype == BF16 else 0.0
     tiny = 2.0 ** -120  # values below fp32's normal numbers are lost
     u = U[dtype]
-    b_value = u * value.abs() + (1 + u) * n * value.abs() + tiny
-    b_slope = u * slope.abs() + (1 + u) * n * size + tiny
+    b_value = u * value.abs() + (1 + u) * (n * value.abs() + lost * z.double().abs()) + tiny
+    b_slope = u * slope.abs() + (1 + u) * (n * size + lost) + tiny
     rows = z.view(-1, 1).contiguous()
     close("value", kda.linear_fwd(rows, one, activation=act)[0].view(-1), value, b_value)
     close("value of one row", kda.linear_fwd(one, rows, activation=act)[0].view(-1), value, b_value)
