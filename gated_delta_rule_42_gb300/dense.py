@@ -12,6 +12,7 @@ captured into CUDA graphs.  Tensors are contiguous, bf16 or fp32.
 from __future__ import annotations
 
 from array import array
+from math import inf
 from operator import attrgetter
 from typing import Optional, Sequence
 
@@ -247,9 +248,9 @@ def _check_list(name, ts, device):
 def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None):
     """Scales the tensors (bf16 and fp32, mixed) so that their global L2 norm is
     at most max_norm: out[i] = tensors[i] * min(1, max_norm / (norm + 1e-6)), in
-    place without ``out``.  Returns the norm before clipping, a 0-d fp32 tensor on
-    the device (nothing is synchronised).  max_norm = inf computes the norm and
-    scales nothing."""
+    place without ``out``; autograd counts it as a modification of what is written.
+    Returns the norm before clipping, a 0-d fp32 tensor on the device (nothing is
+    synchronised).  max_norm = inf computes the norm and scales nothing."""
     tensors = list(tensors)
     if not tensors:
         raise ValueError("clip_grad_norm needs at least one tensor")
@@ -273,4 +274,6 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float, out: Option
     _lib.check(lib, lib.kda_clip_grad_norm(len(tensors), src.buffer_info()[0], dst.buffer_info()[0],
                                            sizes.buffer_info()[0], kinds.buffer_info()[0], max_norm, norm.data_ptr(),
                                            wp, wb, _stream(device)))
+    if out is not None or max_norm != inf:
+        torch.autograd.graph.increment_version(tensors if out is None else out)
     return norm
