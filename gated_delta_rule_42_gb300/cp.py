@@ -29,7 +29,7 @@ from typing import Callable, List, NamedTuple, Optional, Union
 import torch
 
 from . import _lib
-from .ops import (chunk_kda_bwd, chunk_kda_bwd_ctx, chunk_kda_bwd_state, chunk_kda_fwd, chunk_kda_fwd_ctx,
+from .ops import (_stream, chunk_kda_bwd, chunk_kda_bwd_ctx, chunk_kda_bwd_state, chunk_kda_fwd, chunk_kda_fwd_ctx,
                   chunk_kda_fwd_reuse)
 
 
@@ -42,8 +42,7 @@ def compose(M: torch.Tensor, h: torch.Tensor, c: Optional[torch.Tensor], transpo
     p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
     _lib.check(lib, lib.kda_state_compose(p(M.contiguous()), p(h.contiguous()),
                                           p(None if c is None else c.contiguous()), p(out), N * HV, K, V,
-                                          1 if transpose else 0,
-                                          ctypes.c_void_p(torch.cuda.current_stream(h.device).cuda_stream)))
+                                          1 if transpose else 0, _stream(h.device)))
     return out
 
 

@@ -20,7 +20,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .ops import _check_tensor
+from .ops import _check_current, _check_tensor
 
 __all__ = ["layer_norm", "layer_norm_fwd", "layer_norm_bwd", "linear", "linear_fwd", "linear_bwd", "clip_grad_norm"]
 
@@ -34,6 +34,7 @@ def _p(t: Optional[torch.Tensor]):
 
 
 def _stream(device):
+    _check_current(device)
     # the raw handle: a torch.cuda.Stream object costs 2 us, a fifth of a small call
     return torch._C._cuda_getCurrentRawStream(device.index)
 

@@ -46,7 +46,8 @@
  * Ownership: the caller allocates every input, output and workspace buffer;
  * the library never allocates or frees device memory, never synchronises and
  * never reads device data on the host.  Work is enqueued on `stream`
- * (a cudaStream_t; NULL = the legacy default stream).  kda_chunk_bwd
+ * (a cudaStream_t; NULL = the legacy default stream) of the calling thread's
+ * current device, on which every buffer must lie.  kda_chunk_bwd
  * recomputes everything it needs from the inputs; the _ctx pair instead keeps
  * the forward's intermediates in a caller-owned context buffer.
  *
