@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <mutex>
 #include <utility>
 
 #include "kda_internal.cuh"
@@ -100,6 +101,8 @@ __device__ __forceinline__ void stparam(void *p, bool f32, int64_t i, float x) {
 
 // Lets a kernel take `smem` bytes of dynamic shared memory: the attribute is set
 // once per kernel and device (it costs microseconds), again only for more bytes.
+// It only ever grows, checked and set under one lock: a call of a smaller size on
+// another thread must not take it back between a larger call's grant and launch.
 // Up to 40 KB need none, the kernel's static part included.
 template <typename K>
 cudaError_t allow_smem(K kernel, std::atomic<int> (&granted)[64], size_t smem) {
@@ -107,9 +110,13 @@ cudaError_t allow_smem(K kernel, std::atomic<int> (&granted)[64], size_t smem) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && granted[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (granted[dev].load(std::memory_order_acquire) >= (int)smem) return cudaSuccess;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (granted[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) granted[dev].store((int)smem, std::memory_order_relaxed);
+  if (e == cudaSuccess) granted[dev].store((int)smem, std::memory_order_release);
   return e;
 }
 
