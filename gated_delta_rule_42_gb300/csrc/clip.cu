@@ -284,9 +284,11 @@ cudaError_t run(Walk w, int sms, float max_norm, float *norm, double *part, cuda
   Table<CAP> tab;
   int parts = 0;
   Walk again = w;
+  cudaError_t e;  // a pass that was not launched leaves nothing to scale by: the call ends there
   while (w.next(tab)) {
     const int grid = tab.chunks < most ? tab.chunks : most;
     KDA_LAUNCH("clip_norm_kernel", s, start_kernel(clip_norm_kernel<CAP>, grid, kThreads, 0, s, tab, part + parts));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     parts += grid;
   }
   bool first = true;
@@ -295,10 +297,11 @@ cudaError_t run(Walk w, int sms, float max_norm, float *norm, double *part, cuda
     const int grid = tab.chunks < 1 ? 1 : tab.chunks < most ? tab.chunks : most;
     KDA_LAUNCH("clip_scale_kernel", s,
                start_kernel(clip_scale_kernel<CAP>, grid, kThreads, 0, s, tab, part, parts, max_norm, first ? norm : nullptr));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     first = false;
     if (again.out == nullptr) break;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace

@@ -347,9 +347,10 @@ cudaError_t launch_simt(const Product &P, float *part, int sms, cudaStream_t s) 
   DENSE_ACT_SWITCH(P.act, {
     KDA_LAUNCH("linear_simt_kernel", s,
                start_kernel(linear_simt_kernel<ACT>, (unsigned)R.blocks, kSimtThreads, 0, s, P, R, part, grid));
-    if (shares(R))
-      KDA_LAUNCH("simt_join_kernel", s,
-                 start_kernel(simt_join_kernel<ACT>, (unsigned)(R.slices / R.per_tile * (kBM / kJoinRows)), 256, 0, s, P, R, part, grid));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !shares(R)) return e;
+    KDA_LAUNCH("simt_join_kernel", s,
+               start_kernel(simt_join_kernel<ACT>, (unsigned)(R.slices / R.per_tile * (kBM / kJoinRows)), 256, 0, s, P, R, part, grid));
   });
   return cudaGetLastError();
 }

@@ -14,8 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 def run_host(source, tmp_path):
     """Compiles a host program of this folder against the library's sources and runs it."""
     exe = str(tmp_path / "host")
-    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", build.INCLUDE, "-I",
-                    build.CSRC, os.path.join(HERE, source), "-o", exe], check=True, capture_output=True, text=True)
+    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-Xcicc", "-O0", "-Xptxas",
+                    "-O0", "-I", build.INCLUDE, "-I", build.CSRC, os.path.join(HERE, source), "-o", exe], check=True, capture_output=True, text=True)
     return subprocess.run([exe], capture_output=True, text=True, timeout=60)
 
 
