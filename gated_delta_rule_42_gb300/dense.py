@@ -196,8 +196,10 @@ def linear_bwd(dy, x, weight, bias=None, activation: Optional[str] = None, preac
 
 class LinearFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, activation, residual):
-        y, z = linear_fwd(x, weight, bias, activation, residual, keep_preact=any(ctx.needs_input_grad[:3]))
+    def forward(ctx, x, weight, bias, activation, residual, grad_mode):
+        # needs_input_grad is set under no_grad too, and grad mode is always off in here: apply's caller reads it
+        y, z = linear_fwd(x, weight, bias, activation, residual,
+                          keep_preact=grad_mode and any(ctx.needs_input_grad[:3]))
         ctx.save_for_backward(x, weight, bias, z)
         ctx.activation = activation
         return y
@@ -212,12 +214,12 @@ class LinearFunction(torch.autograd.Function):
         if any(need[:3]):
             dx, dw, db = linear_bwd(d, x, weight, bias if need[2] else None, ctx.activation, z, need_dx=need[0],
                                     need_dweight=need[1])
-        return dx, dw, db, None, dy if need[4] else None
+        return dx, dw, db, None, dy if need[4] else None, None
 
 
 def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None):
     """y = act(x weight^T + bias) + residual, with autograd; see :func:`linear_fwd`."""
-    return LinearFunction.apply(x, weight, bias, activation, residual)
+    return LinearFunction.apply(x, weight, bias, activation, residual, torch.is_grad_enabled())
 
 
 # ---- gradient clipping ------------------------------------------------------------
