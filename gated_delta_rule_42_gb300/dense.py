@@ -11,6 +11,7 @@ captured into CUDA graphs.  Tensors are contiguous, bf16 or fp32.
 """
 from __future__ import annotations
 
+import ctypes
 from array import array
 from math import inf
 from operator import attrgetter
@@ -26,6 +27,7 @@ __all__ = ["layer_norm", "layer_norm_fwd", "layer_norm_bwd", "linear", "linear_f
 
 _DTYPE = {torch.float32: _lib.KDA_F32, torch.bfloat16: _lib.KDA_BF16}
 _dtype_of = attrgetter("dtype")
+_SIZE_MAX = ctypes.c_size_t(-1).value
 _ACT = {None: 0, "silu": 1, "gelu": 2, "sigmoid": 3}
 
 
@@ -44,6 +46,12 @@ def _scratch(nbytes: int, device):
     ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     at = (ws.data_ptr() + 255) & ~255
     return ws, at, nbytes
+
+
+def _workspace(need: int, device):
+    """_scratch, or none where none is needed.  SIZE_MAX marks a problem that the library refuses: the call itself
+    then raises its message."""
+    return _scratch(need, device) if 0 < need < _SIZE_MAX else (None, None, 0)
 
 
 def _check_input(name, t):
@@ -163,8 +171,7 @@ def linear_fwd(x, weight, bias=None, activation: Optional[str] = None, residual=
     s = _linear_struct(x, weight, bias, residual, activation)
     y = torch.empty(x.shape[:-1] + (s.outs,), dtype=x.dtype, device=x.device)
     z = torch.empty_like(y) if keep_preact and activation is not None else None
-    need = lib.kda_linear_fwd_workspace_size(s)
-    ws, wp, wb = _scratch(need, x.device) if need else (None, None, 0)
+    ws, wp, wb = _workspace(lib.kda_linear_fwd_workspace_size(s), x.device)
     _lib.check(lib, lib.kda_linear_fwd(s, y.data_ptr(), _p(z), wp, wb, _stream(x.device)))
     return y, z
 
@@ -187,8 +194,7 @@ def linear_bwd(dy, x, weight, bias=None, activation: Optional[str] = None, preac
     db = None if bias is None else torch.empty_like(bias)
     if dx is None and dw is None and db is None:
         return None, None, None
-    need = lib.kda_linear_bwd_workspace_size(s)
-    ws, wp, wb = _scratch(need, x.device) if need else (None, None, 0)
+    ws, wp, wb = _workspace(lib.kda_linear_bwd_workspace_size(s), x.device)
     _lib.check(lib, lib.kda_linear_bwd(s, dy.data_ptr(), _p(preact), _p(dx), _p(dw), _p(db), wp, wb,
                                        _stream(x.device)))
     return dx, dw, db

@@ -51,3 +51,16 @@ def test_the_preactivation_is_kept_for_a_backward(kept, monkeypatch):
     y.sum().backward()
     assert kept == [True] and calls == [(True, False, True)]
     assert (w.grad == 1).all() and (b.grad == 1).all()
+
+
+def test_a_problem_too_large_says_so(monkeypatch):
+    """The library's refusal reaches the caller, not the allocator's error on a workspace of SIZE_MAX bytes."""
+    from gated_delta_rule_42_gb300 import _lib, build
+    build.build()
+    monkeypatch.setattr(dense, "_check_input", lambda name, t: None)
+    monkeypatch.setattr(dense, "_stream", lambda device: None)
+    x = torch.empty(1, (1 << 24) + 8, dtype=torch.bfloat16)
+    with pytest.raises(_lib.KdaError, match="linear: problem too large"):
+        dense.linear_fwd(x, x)
+    with pytest.raises(_lib.KdaError, match="linear: problem too large"):
+        dense.linear_bwd(torch.empty(1, 1, dtype=torch.bfloat16), x, x)
