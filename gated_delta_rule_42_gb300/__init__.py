@@ -8,4 +8,4 @@ first use and its absence is an error (there is no fallback path)."""
 from .ops import (chunk_kda, chunk_kda_bwd, chunk_kda_bwd_ctx, chunk_kda_bwd_state, chunk_kda_fwd,  # noqa: F401
                   chunk_kda_fwd_ctx, recurrent_kda)
 from .dense import (clip_grad_norm, layer_norm, layer_norm_bwd, layer_norm_fwd, linear, linear_bwd,  # noqa: F401
-                    linear_fwd)
+                    linear_fwd, linear_status)

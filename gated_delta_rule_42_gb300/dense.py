@@ -23,7 +23,8 @@ from torch.autograd.function import once_differentiable
 from . import _lib
 from .ops import _check_current, _check_tensor
 
-__all__ = ["layer_norm", "layer_norm_fwd", "layer_norm_bwd", "linear", "linear_fwd", "linear_bwd", "clip_grad_norm"]
+__all__ = ["layer_norm", "layer_norm_fwd", "layer_norm_bwd", "linear", "linear_fwd", "linear_bwd", "linear_status",
+           "clip_grad_norm"]
 
 _DTYPE = {torch.float32: _lib.KDA_F32, torch.bfloat16: _lib.KDA_BF16}
 _dtype_of = attrgetter("dtype")
@@ -226,6 +227,25 @@ class LinearFunction(torch.autograd.Function):
 def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None):
     """y = act(x weight^T + bias) + residual, with autograd; see :func:`linear_fwd`."""
     return LinearFunction.apply(x, weight, bias, activation, residual, torch.is_grad_enabled())
+
+
+class _DeviceWord:
+    def __init__(self, address: int):
+        self.__cuda_array_interface__ = {"shape": (), "typestr": "<i4", "data": (address, False), "version": 2}
+
+
+def linear_status(device="cuda"):
+    """A 0-d int32 tensor on the device: nonzero if a bounded device wait of a linear call
+    gave up by this point of the current stream (the results of such a call are invalid).
+    The word is never cleared.  Nothing is synchronised: reading the tensor is the caller's
+    moment to wait, once a step or once a run."""
+    device = torch.device(device)
+    if device.index is not None:
+        _check_current(device)
+    lib = _lib.load()
+    word = ctypes.c_void_p()
+    _lib.check(lib, lib.kda_linear_status(ctypes.byref(word)))
+    return torch.as_tensor(_DeviceWord(word.value), device=device).clone()
 
 
 # ---- gradient clipping ------------------------------------------------------------
