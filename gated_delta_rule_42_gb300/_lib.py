@@ -27,7 +27,7 @@ EXPORTS = (
     "kda_status_offset", "kda_debug_bounded_wait", "kda_uses_tensor_cores",
     "kda_layer_norm_fwd", "kda_layer_norm_bwd_workspace_size", "kda_layer_norm_bwd",
     "kda_linear_fwd_workspace_size", "kda_linear_bwd_workspace_size", "kda_linear_fwd", "kda_linear_bwd",
-    "kda_clip_grad_norm_workspace_size", "kda_clip_grad_norm", "kda_linear_status",
+    "kda_clip_grad_norm_workspace_size", "kda_clip_grad_norm", "kda_linear_status", "kda_debug_linear_waits",
 )
 
 
@@ -129,6 +129,8 @@ def load(path: str = LIB_PATH):
             getattr(lib, nm).restype = sz
         lib.kda_linear_status.argtypes = [ctypes.POINTER(vp)]
         lib.kda_linear_status.restype = i
+        lib.kda_debug_linear_waits.argtypes = [L, vp, vp, sz, vp, ctypes.c_longlong, vp]
+        lib.kda_debug_linear_waits.restype = i
         lib.kda_clip_grad_norm.argtypes = [i, vp, vp, vp, vp, ctypes.c_float, vp, vp, sz, vp]
         lib.kda_clip_grad_norm.restype = i
         lib.kda_status_string.argtypes = [i]

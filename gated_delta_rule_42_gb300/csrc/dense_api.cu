@@ -144,6 +144,22 @@ kda_status kda_linear_fwd(const kda_linear *p, void *y, void *preact, void *work
               "kda_linear_fwd");
 }
 
+kda_status kda_debug_linear_waits(const kda_linear *p, void *y, void *workspace, size_t workspace_bytes, int *err,
+                                  long long polls, void *stream) {
+  Linear L{};
+  kda_status st = check_linear(p, L);
+  if (st != KDA_OK) return st;
+  if (!linear_uses_tensor_cores(L)) return fail(KDA_ERR_UNSUPPORTED, "linear waits: not a tensor-core forward");
+  if (y == nullptr || err == nullptr || misaligned(y, true) || misaligned(err, false))
+    return fail(KDA_ERR_INVALID_ARG, "linear waits: y and err are required");
+  if (polls < 0 || polls > umma::kSpinLimit)
+    return fail(KDA_ERR_INVALID_ARG, "linear waits: polls must be 0 .. %ld", umma::kSpinLimit);
+  if ((st = workspace_ok(workspace, workspace_bytes, linear_fwd_workspace(L))) != KDA_OK) return st;
+  return done(launch_linear_fwd(L, y, nullptr, static_cast<char *>(workspace), (cudaStream_t)stream,
+                                Waits{(long)polls, err}),
+              "kda_debug_linear_waits");
+}
+
 kda_status kda_linear_bwd(const kda_linear *p, const void *dy, const void *preact, void *dx, void *dweight,
                           void *dbias, void *workspace, size_t workspace_bytes, void *stream) {
   Linear L{};

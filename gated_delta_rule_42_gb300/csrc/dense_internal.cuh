@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "kda_internal.cuh"
+#include "umma.cuh"
 
 namespace kda {
 namespace dense {
@@ -263,11 +264,20 @@ struct Linear {
   int act;
   const void *x, *weight, *bias, *residual;
 };
+// The bounds of a tensor-core product's waits: polls each, and the device word that
+// a wait that gave up sets to 1 (NULL: the library's own, linear_status_word).
+struct Waits {
+  long polls;
+  int *err;
+};
+constexpr Waits kWaits{umma::kSpinLimit, nullptr};
 // Device word that is nonzero once a bounded wait of a product gave up.
 cudaError_t linear_status_word(int **p);
 size_t linear_fwd_workspace(const Linear &L);
 size_t linear_bwd_workspace(const Linear &L);
-cudaError_t launch_linear_fwd(const Linear &L, void *y, void *preact, char *ws, cudaStream_t s);
+cudaError_t launch_linear_fwd(const Linear &L, void *y, void *preact, char *ws, cudaStream_t s,
+                              const Waits &waits = kWaits);
+bool linear_uses_tensor_cores(const Linear &L);  // its forward
 cudaError_t launch_linear_bwd(const Linear &L, const void *dy, const void *preact, void *dx, void *dweight,
                               void *dbias, char *ws, cudaStream_t s);
 

@@ -172,8 +172,8 @@ size_t part_bytes(int64_t M, int64_t N, int64_t K, bool bf16, int sms) {
 }
 
 // One product with its epilogue.
-cudaError_t product(const Product &P, bool bf16, float *part, int sms, cudaStream_t s) {
-  return bf16 ? launch_tc(P, part, sms, s) : launch_simt(P, part, sms, s);
+cudaError_t product(const Product &P, bool bf16, float *part, int sms, cudaStream_t s, const Waits &waits = kWaits) {
+  return bf16 ? launch_tc(P, part, sms, s, waits) : launch_simt(P, part, sms, s);
 }
 
 // Up to 32 bf16 rows on the 16-byte grid, 16 off it, and 16 fp32 rows stream the
@@ -230,7 +230,9 @@ BwdLayout bwd_layout(const Linear &L, int sms) {
 size_t linear_fwd_workspace(const Linear &L) { return fwd_layout(L, sms_or_default()).total; }
 size_t linear_bwd_workspace(const Linear &L) { return bwd_layout(L, sms_or_default()).total; }
 
-cudaError_t launch_linear_fwd(const Linear &L, void *y, void *preact, char *ws, cudaStream_t s) {
+bool linear_uses_tensor_cores(const Linear &L) { return L.bf16 && L.rows > 0 && !few_rows(L); }
+
+cudaError_t launch_linear_fwd(const Linear &L, void *y, void *preact, char *ws, cudaStream_t s, const Waits &waits) {
   if (L.rows == 0) return cudaSuccess;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
@@ -245,7 +247,7 @@ cudaError_t launch_linear_fwd(const Linear &L, void *y, void *preact, char *ws, 
     P.a = g.x;
     P.b = g.w;
   }
-  return product(P, L.bf16, reinterpret_cast<float *>(ws + f.part), sms, s);
+  return product(P, L.bf16, reinterpret_cast<float *>(ws + f.part), sms, s, waits);
 }
 
 cudaError_t launch_linear_bwd(const Linear &L, const void *dy, const void *preact, void *dx, void *dweight,

@@ -85,7 +85,7 @@ cudaError_t launch_few32(const Product &P, cudaStream_t s);
 // Product of the tensor cores (linear_tc.cu): bf16 operands whose base and rows
 // lie on 16-byte boundaries, K >= 1, the epilogue and the join included.
 size_t tc_part_bytes(int64_t M, int64_t N, int64_t K, int sms);
-cudaError_t launch_tc(const Product &P, float *part, int sms, cudaStream_t s);
+cudaError_t launch_tc(const Product &P, float *part, int sms, cudaStream_t s, const Waits &waits);
 
 // Product of a few rows (linear_few.cu): bf16, M <= kFewRows, both operands with
 // k contiguous and rows K apart (any alignment); no workspace.

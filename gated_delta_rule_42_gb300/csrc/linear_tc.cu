@@ -39,6 +39,8 @@ constexpr int stage_bytes(int bn) { return kABytes + b_bytes(bn); }
 struct Shared {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
+  uint32_t gave_up;  // a wait of either CTA did
+  uint32_t issued;   // stages that this CTA's loading warp issued
 };
 constexpr int smem_bytes(int bn) {
   return 1024 /* alignment */ + kStages * stage_bytes(bn) + kEpilogueWarps * 4096 + 256;
@@ -60,7 +62,9 @@ struct TcArgs {
   Schedule s;
   float *part;  // [tiles - whole][splits][256][bn]
   int row_tiles, col_tiles;
-  bool grid;  // output rows on 16-byte boundaries
+  bool grid;   // output rows on 16-byte boundaries
+  long polls;  // limit of a wait, and where one that gave up leaves 1 (NULL: g_gave_up)
+  int *err;
 };
 
 struct Unit {
@@ -183,6 +187,35 @@ __device__ __forceinline__ void store_part(float *tile, const unsigned char *sm,
   }
 }
 
+// After a wait that gave up, once both CTAs' roles have ended: the products and the
+// copies that are still in flight are waited for, since they read and write shared
+// and tensor memory that ends with the block.  The leader does it for both: its
+// barriers count both CTAs' copies.  A CTA may have issued up to kStages stages
+// that the other did not (no stage is issued again before it was consumed, which
+// takes both CTAs' halves): their barriers lack the other's bytes, or the leader's
+// own arrival, which are made up for first.
+__device__ __forceinline__ void settle(Shared &sh, int warp, uint32_t stage_bytes, int *err) {
+  if (warp == kEpilogueWarps + 1) {
+    if (pair::elect()) pair::commit(&sh.drain);  // the lane that issued the products
+    __syncwarp();
+    pair::wait_cluster(&sh.drain, 0, err, umma::kSpinLimit);
+  } else if (warp == kEpilogueWarps && pair::elect()) {
+    const int n0 = (int)sh.issued, n1 = (int)pair::load_at(&sh.issued, 1);
+    for (int s = 0; s < kStages; ++s) {
+      // the last stage of this slot that each has issued, or below 0
+      const int last0 = n0 - 1 - (n0 - 1 - s + kStages) % kStages, last1 = n1 - 1 - (n1 - 1 - s + kStages) % kStages;
+      const int last = last0 > last1 ? last0 : last1;
+      if (last < 0) continue;
+      if (last1 < last)
+        pair::complete_tx(&sh.full[s], stage_bytes);
+      else if (last0 < last)
+        pair::arrive_expect(&sh.full[s], stage_bytes);
+      pair::wait_cluster(&sh.full[s], (last / kStages) & 1, err, umma::kSpinLimit);
+    }
+  }
+  __syncwarp();
+}
+
 template <bool AK, bool BK, int ACT, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a,
@@ -205,6 +238,7 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
       umma::bar_init(&sh.acc_empty[i], 2 * kEpilogueWarps);
     }
     umma::bar_init(&sh.drain, 1);
+    sh.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 0) pair::tmem_alloc(&sh.tmem, kTmemCols);
@@ -219,6 +253,8 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
   wait_for_stream();  // all above is the block's own
   const uint32_t tmem = sh.tmem;
   const uint32_t base = umma::smem_u32(tiles);
+  int *const err = a.err != nullptr ? a.err : &g_gave_up;
+  bool ok = true;  // no wait of this warp gave up
 
   // The two issuing warps stay converged and elect a lane for each instruction: a
   // lane alone in a divergent branch issues them so slowly that the pipe waits
@@ -226,14 +262,13 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
   // loads).
   if (warp == kEpilogueWarps) {  // TMA, both CTAs
     uint32_t it = 0;
-    bool ok = true;
     for (int u = first; u < units && ok; u += stride) {
       const Unit w = unit_of(a, u);
       const int m = (int)w.m0 + (int)rank * kHalf, n = (int)w.n0 + (int)rank * (BN / 2);
       for (int kb = 0; kb < w.k_count; ++kb, ++it) {
         const int s = it % kStages;
         if (it >= kStages &&
-            !__all_sync(0xffffffffu, pair::wait_cluster(&sh.empty[s], (it / kStages - 1) & 1, &g_gave_up))) {
+            !__all_sync(0xffffffffu, pair::wait_cluster(&sh.empty[s], (it / kStages - 1) & 1, err, a.polls))) {
           ok = false;
           break;
         }
@@ -258,27 +293,24 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
         __syncwarp();
       }
     }
-    if (!ok && rank == 0) {  // gave up: let the copies in flight land before the block's memory goes
-      const uint32_t from = it > kStages ? it - kStages : 0;
-      for (uint32_t i = from; i < it; ++i) pair::wait_cluster(&sh.full[i % kStages], (i / kStages) & 1, &g_gave_up);
-    }
+    if (lane == 0) sh.issued = it;
   } else if (warp == kEpilogueWarps + 1) {  // products, leader CTA
     if (rank == 0) {
       const uint32_t idesc = umma::idesc_bf16(kTile, BN) | (AK ? 0u : 1u << 15) | (BK ? 0u : 1u << 16);
       const uint32_t d0 = __shfl_sync(0xffffffffu, tmem, 0);
       uint32_t it = 0, tile = 0;
-      bool ok = true, have = false;  // have: the stage's data was seen to be there
+      bool have = false;  // have: the stage's data was seen to be there
       for (int u = first; u < units && ok; u += stride, ++tile) {
         const int count = unit_of(a, u).k_count;
         const int acc = tile & 1;
-        if (tile >= 2 && !__all_sync(0xffffffffu, pair::wait_cluster(&sh.acc_empty[acc], (tile / 2 - 1) & 1, &g_gave_up))) {
+        if (tile >= 2 && !__all_sync(0xffffffffu, pair::wait_cluster(&sh.acc_empty[acc], (tile / 2 - 1) & 1, err, a.polls))) {
           ok = false;
           break;
         }
         umma::fence_after();
         for (int kb = 0; kb < count; ++kb, ++it) {
           const int s = it % kStages;
-          if (!__all_sync(0xffffffffu, have || pair::wait_cluster(&sh.full[s], (it / kStages) & 1, &g_gave_up))) {
+          if (!__all_sync(0xffffffffu, have || pair::wait_cluster(&sh.full[s], (it / kStages) & 1, err, a.polls))) {
             ok = false;
             break;
           }
@@ -298,11 +330,6 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
           __syncwarp();
         }
       }
-      if (!ok) {  // products still in flight read shared memory and write tensor memory
-        if (pair::elect()) pair::commit_both(&sh.drain);
-        __syncwarp();
-        pair::wait_cluster(&sh.drain, 0, &g_gave_up);
-      }
     }
   } else {  // epilogue: warp w reads lanes 32 (w % 4) of its CTA's tensor memory, half of the columns
     const int quarter = warp & 3, side = warp >> 2;
@@ -311,7 +338,10 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
     for (int u = first; u < units; u += stride, ++tile) {
       const Unit w = unit_of(a, u);
       const int acc = tile & 1;
-      if (!__all_sync(0xffffffffu, pair::wait_cluster(&sh.acc_full[acc], (tile / 2) & 1, &g_gave_up))) break;
+      if (!__all_sync(0xffffffffu, pair::wait_cluster(&sh.acc_full[acc], (tile / 2) & 1, err, a.polls))) {
+        ok = false;
+        break;
+      }
       umma::fence_after();
       const int row0 = rank * kHalf + quarter * 32;
       const int64_t m0 = w.m0 + row0;
@@ -345,11 +375,20 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
       }
     }
   }
+  if (!ok && lane == 0) {
+    pair::store_at(&sh.gave_up, 0, 1);
+    pair::store_at(&sh.gave_up, 1, 1);
+  }
   __syncwarp();
   umma::fence_before();
   __syncthreads();
   pair::cluster_sync();
   umma::fence_after();
+  if (sh.gave_up != 0) {  // the same in both CTAs
+    if (rank == 0) settle(sh, warp, kStageBytes, err);
+    __syncthreads();
+    pair::cluster_sync();
+  }
   if (warp == 0) pair::tmem_free(tmem, kTmemCols);
 }
 
@@ -488,9 +527,9 @@ cudaError_t linear_status_word(int **p) {
 
 size_t tc_part_bytes(int64_t M, int64_t N, int64_t K, int sms) { return part_bytes_of(schedule_of(M, N, K, sms)); }
 
-cudaError_t launch_tc(const Product &P, float *part, int sms, cudaStream_t s) {
+cudaError_t launch_tc(const Product &P, float *part, int sms, cudaStream_t s, const Waits &waits) {
   const Schedule S = schedule_of(P.M, P.N, P.K, sms);
-  const TcArgs a{P, S, part, (int)tiles_of(P.M, kTile), (int)tiles_of(P.N, S.bn), rows_on_grid(P)};
+  const TcArgs a{P, S, part, (int)tiles_of(P.M, kTile), (int)tiles_of(P.N, S.bn), rows_on_grid(P), waits.polls, waits.err};
   CUtensorMap ma, mb;
   cudaError_t e = operand_map(&ma, P.a, P.M, P.K, kHalf);
   if (e == cudaSuccess) e = operand_map(&mb, P.b, P.N, P.K, S.bn / 2);

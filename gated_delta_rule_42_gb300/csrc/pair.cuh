@@ -34,10 +34,24 @@ __device__ __forceinline__ void arrive_expect(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(umma::smem_u32(bar)), "r"(bytes)
                : "memory");
 }
+// Counts bytes that no copy will bring (the peer CTA ended before it issued its own).
+__device__ __forceinline__ void complete_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(umma::smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
+// A word of the CTA `rank`'s shared memory.
+__device__ __forceinline__ void store_at(uint32_t *p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(at_rank(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t load_at(const uint32_t *p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(at_rank(p, rank)) : "memory");
+  return v;
+}
 // Bounded wait that also acquires what the peer CTA released (tensor memory
 // handed back, barriers of the pair).
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, int *err) {
-  for (long it = 0; it < umma::kSpinLimit; ++it) {
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, int *err, long polls) {
+  for (long it = 0; it < polls; ++it) {
     uint32_t ok;
     asm volatile(
         "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
@@ -106,6 +120,12 @@ __device__ __forceinline__ void commit_both(uint64_t *bar) {
           umma::smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
+}
+// The same in this CTA alone.
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
+                   umma::smem_u32(bar))
+               : "memory");
 }
 
 // Operand with its rows contiguous (MN-major), 128-byte swizzle: blocks of 64

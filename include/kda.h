@@ -380,12 +380,13 @@ const char *kda_status_string(kda_status s);
 /* Message describing the last failure on the calling thread ("" if none). */
 const char *kda_last_error(void);
 
-/* Library ABI version (major * 100 + minor): 108 (101: kda_inputs gained
+/* Library ABI version (major * 100 + minor): 109 (101: kda_inputs gained
  * `flags`; 102: the forward-context entry points; 103: the final-state-only
  * forward, the start-state-gradient-only backward, kda_chunk_fwd_reuse; 104:
  * kda_status_offset, kda_debug_bounded_wait; 105: status words 3 and 4,
  * kda_uses_tensor_cores; 106: KDA_GATE_IN_KERNEL and kda_inputs.gate; 107:
- * status words 5 and 6; 108: layer norm, linear, gradient clipping). */
+ * status words 5 and 6; 108: layer norm, linear, gradient clipping; 109:
+ * kda_debug_linear_waits). */
 int kda_version(void);
 
 /* Chunked forward without a caller workspace (no counterpart on the pages).
@@ -413,6 +414,15 @@ kda_status kda_chunk_fwd_noalloc(const kda_inputs *in, void *o, float *hT, void 
  * int) to 1, the way a kernel of this library reports a copy that never
  * arrived.  For tests of that path; it neither faults nor hangs the GPU. */
 kda_status kda_debug_bounded_wait(int *err, long long polls, void *stream);
+
+/* kda_linear_fwd of a bf16 problem that runs on the tensor cores (more than 32
+ * rows), with every wait of its pipeline given up after `polls` polls (0 .. 2^24,
+ * its usual limit): a wait that gives up sets *err (a device int) to 1, not the
+ * word of kda_linear_status, and y is then invalid.  For tests of that path; the
+ * kernel waits for what it has in flight and returns, it neither faults nor hangs
+ * the GPU. */
+kda_status kda_debug_linear_waits(const kda_linear *p, void *y, void *workspace, size_t workspace_bytes, int *err,
+                                  long long polls, void *stream);
 
 /* Kernels launched by this library in this process so far. */
 unsigned long long kda_launch_count(void);
