@@ -156,7 +156,7 @@ kda_status kda_debug_linear_waits(const kda_linear *p, void *y, void *workspace,
     return fail(KDA_ERR_INVALID_ARG, "linear waits: polls must be 0 .. %ld", umma::kSpinLimit);
   if ((st = workspace_ok(workspace, workspace_bytes, linear_fwd_workspace(L))) != KDA_OK) return st;
   return done(launch_linear_fwd(L, y, nullptr, static_cast<char *>(workspace), (cudaStream_t)stream,
-                                Waits{(long)polls, err}),
+                                Waits{(int)polls, err}),
               "kda_debug_linear_waits");
 }
 

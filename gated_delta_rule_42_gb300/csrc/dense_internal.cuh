@@ -267,10 +267,10 @@ struct Linear {
 // The bounds of a tensor-core product's waits: polls each, and the device word that
 // a wait that gave up sets to 1 (NULL: the library's own, linear_status_word).
 struct Waits {
-  long polls;
+  int polls;
   int *err;
 };
-constexpr Waits kWaits{umma::kSpinLimit, nullptr};
+constexpr Waits kWaits{(int)umma::kSpinLimit, nullptr};
 // Device word that is nonzero once a bounded wait of a product gave up.
 cudaError_t linear_status_word(int **p);
 size_t linear_fwd_workspace(const Linear &L);

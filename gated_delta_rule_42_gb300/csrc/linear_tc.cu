@@ -63,7 +63,7 @@ struct TcArgs {
   float *part;  // [tiles - whole][splits][256][bn]
   int row_tiles, col_tiles;
   bool grid;   // output rows on 16-byte boundaries
-  long polls;  // limit of a wait, and where one that gave up leaves 1 (NULL: g_gave_up)
+  int polls;   // limit of a wait, and where one that gave up leaves 1 (NULL: g_gave_up)
   int *err;
 };
 
@@ -187,6 +187,12 @@ __device__ __forceinline__ void store_part(float *tile, const unsigned char *sm,
   }
 }
 
+__device__ __forceinline__ bool wait(const TcArgs &a, uint64_t *bar, uint32_t parity, int polls) {
+  if (pair::wait_cluster(bar, parity, polls)) return true;
+  atomicExch(a.err != nullptr ? a.err : &g_gave_up, 1);
+  return false;
+}
+
 // After a wait that gave up, once both CTAs' roles have ended: the products and the
 // copies that are still in flight are waited for, since they read and write shared
 // and tensor memory that ends with the block.  The leader does it for both: its
@@ -194,11 +200,11 @@ __device__ __forceinline__ void store_part(float *tile, const unsigned char *sm,
 // that the other did not (no stage is issued again before it was consumed, which
 // takes both CTAs' halves): their barriers lack the other's bytes, or the leader's
 // own arrival, which are made up for first.
-__device__ __forceinline__ void settle(Shared &sh, int warp, uint32_t stage_bytes, int *err) {
+__device__ __forceinline__ void settle(const TcArgs &a, Shared &sh, int warp, uint32_t stage_bytes) {
   if (warp == kEpilogueWarps + 1) {
     if (pair::elect()) pair::commit(&sh.drain);  // the lane that issued the products
     __syncwarp();
-    pair::wait_cluster(&sh.drain, 0, err, umma::kSpinLimit);
+    wait(a, &sh.drain, 0, (int)umma::kSpinLimit);
   } else if (warp == kEpilogueWarps && pair::elect()) {
     const int n0 = (int)sh.issued, n1 = (int)pair::load_at(&sh.issued, 1);
     for (int s = 0; s < kStages; ++s) {
@@ -210,7 +216,7 @@ __device__ __forceinline__ void settle(Shared &sh, int warp, uint32_t stage_byte
         pair::complete_tx(&sh.full[s], stage_bytes);
       else if (last0 < last)
         pair::arrive_expect(&sh.full[s], stage_bytes);
-      pair::wait_cluster(&sh.full[s], (last / kStages) & 1, err, umma::kSpinLimit);
+      wait(a, &sh.full[s], (last / kStages) & 1, (int)umma::kSpinLimit);
     }
   }
   __syncwarp();
@@ -253,7 +259,6 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
   wait_for_stream();  // all above is the block's own
   const uint32_t tmem = sh.tmem;
   const uint32_t base = umma::smem_u32(tiles);
-  int *const err = a.err != nullptr ? a.err : &g_gave_up;
   bool ok = true;  // no wait of this warp gave up
 
   // The two issuing warps stay converged and elect a lane for each instruction: a
@@ -268,7 +273,7 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
       for (int kb = 0; kb < w.k_count; ++kb, ++it) {
         const int s = it % kStages;
         if (it >= kStages &&
-            !__all_sync(0xffffffffu, pair::wait_cluster(&sh.empty[s], (it / kStages - 1) & 1, err, a.polls))) {
+            !__all_sync(0xffffffffu, wait(a, &sh.empty[s], (it / kStages - 1) & 1, a.polls))) {
           ok = false;
           break;
         }
@@ -303,14 +308,14 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
       for (int u = first; u < units && ok; u += stride, ++tile) {
         const int count = unit_of(a, u).k_count;
         const int acc = tile & 1;
-        if (tile >= 2 && !__all_sync(0xffffffffu, pair::wait_cluster(&sh.acc_empty[acc], (tile / 2 - 1) & 1, err, a.polls))) {
+        if (tile >= 2 && !__all_sync(0xffffffffu, wait(a, &sh.acc_empty[acc], (tile / 2 - 1) & 1, a.polls))) {
           ok = false;
           break;
         }
         umma::fence_after();
         for (int kb = 0; kb < count; ++kb, ++it) {
           const int s = it % kStages;
-          if (!__all_sync(0xffffffffu, have || pair::wait_cluster(&sh.full[s], (it / kStages) & 1, err, a.polls))) {
+          if (!__all_sync(0xffffffffu, have || wait(a, &sh.full[s], (it / kStages) & 1, a.polls))) {
             ok = false;
             break;
           }
@@ -338,7 +343,7 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
     for (int u = first; u < units; u += stride, ++tile) {
       const Unit w = unit_of(a, u);
       const int acc = tile & 1;
-      if (!__all_sync(0xffffffffu, pair::wait_cluster(&sh.acc_full[acc], (tile / 2) & 1, err, a.polls))) {
+      if (!__all_sync(0xffffffffu, wait(a, &sh.acc_full[acc], (tile / 2) & 1, a.polls))) {
         ok = false;
         break;
       }
@@ -385,7 +390,7 @@ linear_tc_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ CUten
   pair::cluster_sync();
   umma::fence_after();
   if (sh.gave_up != 0) {  // the same in both CTAs
-    if (rank == 0) settle(sh, warp, kStageBytes, err);
+    if (rank == 0) settle(a, sh, warp, kStageBytes);
     __syncthreads();
     pair::cluster_sync();
   }

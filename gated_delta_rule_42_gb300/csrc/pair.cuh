@@ -50,8 +50,8 @@ __device__ __forceinline__ uint32_t load_at(const uint32_t *p, uint32_t rank) {
 }
 // Bounded wait that also acquires what the peer CTA released (tensor memory
 // handed back, barriers of the pair).
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, int *err, long polls) {
-  for (long it = 0; it < polls; ++it) {
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, int polls) {
+  for (int it = 0; it < polls; ++it) {
     uint32_t ok;
     asm volatile(
         "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
@@ -61,7 +61,6 @@ __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, int
         : "memory");
     if (ok) return true;
   }
-  atomicExch(err, 1);
   return false;
 }
 
