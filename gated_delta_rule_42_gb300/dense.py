@@ -274,20 +274,13 @@ def _check_list(name, ts, device):
     return array("i", kinds), array("q", map(T.numel, ts)), array("Q", map(T.data_ptr, ts))
 
 
-def _refuse_shared(name, ts):
-    first = {}
-    for i, t in enumerate(ts):
-        if t.numel() and first.setdefault(t.data_ptr(), i) != i:
-            raise ValueError(f"{name}[{i}] shares its memory with {name}[{first[t.data_ptr()]}]")
-
-
 def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None):
     """Scales the tensors (bf16 and fp32, mixed) so that their global L2 norm is
     at most max_norm: out[i] = tensors[i] * min(1, max_norm / (norm + 1e-6)), in
     place without ``out``; autograd counts it as a modification of what is written.
     Returns the norm before clipping, a 0-d fp32 tensor on the device (nothing is
     synchronised).  max_norm = inf computes the norm and scales nothing.  What is
-    written must not overlap: a tensor may be read twice, but is written once."""
+    written must not overlap (a tensor may be read twice, but is written once)."""
     tensors = list(tensors)
     if not tensors:
         raise ValueError("clip_grad_norm needs at least one tensor")
@@ -306,9 +299,6 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float, out: Option
         out_kinds, out_sizes, dst = _check_list("out", out, device)
         if out_kinds != kinds or out_sizes != sizes:
             raise ValueError("out must have the tensors' types and sizes")
-    # two blocks would scale the same elements in no order (empty tensors may share an address)
-    if len(set(dst)) != len(dst):
-        _refuse_shared("tensors" if out is None else "out", tensors if out is None else out)
     norm = torch.empty((), dtype=torch.float32, device=device)
     ws, wp, wb = _scratch(lib.kda_clip_grad_norm_workspace_size(len(tensors)), device)
     _lib.check(lib, lib.kda_clip_grad_norm(len(tensors), src.buffer_info()[0], dst.buffer_info()[0],

@@ -17,11 +17,20 @@ def _built():
 
 def test_a_tensor_is_written_once():
     a, b = torch.ones(8, device="cuda"), torch.ones(8, device="cuda")
-    with pytest.raises(ValueError, match=r"tensors\[2\] shares its memory with tensors\[0\]"):
+    with pytest.raises(RuntimeError, match="outputs 0 and 2 overlap"):
         kda.clip_grad_norm([a, b, a], 1.0)
-    with pytest.raises(ValueError, match=r"out\[1\] shares its memory with out\[0\]"):
+    with pytest.raises(RuntimeError, match="outputs 0 and 1 overlap"):
         kda.clip_grad_norm([a, b], 1.0, out=[b, b])
+    with pytest.raises(RuntimeError, match="outputs 1 and 0 overlap"):
+        kda.clip_grad_norm([a[4:], a[:5]], 1.0)
     assert (a == 1).all() and (b == 1).all()
+
+
+def test_views_of_one_buffer_in_any_order():
+    for cuts in ([(0, 4), (4, 8), (8, 16)], [(8, 16), (0, 4), (4, 8)], [(4, 8), (4, 4), (8, 16), (0, 4), (8, 8)]):
+        a = torch.ones(16, device="cuda")
+        assert float(kda.clip_grad_norm([a[i:j] for i, j in cuts], 2.0)) == 4.0
+        assert torch.allclose(a, torch.full_like(a, 0.5))
 
 
 def test_a_tensor_is_read_twice():
