@@ -114,14 +114,17 @@ def make_inputs_struct(q, k, v, g, beta, initial_state=None, cu_seqlens=None, us
     return s
 
 
-def _check_current(device):
-    """The library launches on the thread's current device: tensors of another one would be addressed there."""
-    if torch._C._cuda_getDevice() != device.index:
-        raise ValueError(f"the tensors are on {device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+_current_device = torch._C._cuda_getDevice
+
+
+def _refuse_device(device):
+    raise ValueError(f"the tensors are on {device}, but the current device is cuda:{_current_device()}")
 
 
 def _stream(device):
-    _check_current(device)
+    # the library launches on the thread's current device: tensors of another one would be addressed there
+    if _current_device() != device.index:
+        _refuse_device(device)
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 

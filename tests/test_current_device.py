@@ -7,9 +7,14 @@ import gated_delta_rule_42_gb300 as kda
 from gated_delta_rule_42_gb300 import cp, dense, inputs, ops
 
 
+def current(monkeypatch, index):
+    for module in (ops, dense):
+        monkeypatch.setattr(module, "_current_device", lambda: index)
+
+
 @pytest.mark.parametrize("stream", [ops._stream, dense._stream])
 def test_another_device_is_refused(stream, monkeypatch):
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    current(monkeypatch, 0)
     with pytest.raises(ValueError, match="on cuda:1, but the current device is cuda:0"):
         stream(torch.device("cuda", 1))
 
@@ -33,7 +38,7 @@ def test_every_call_refuses(monkeypatch):
              lambda: kda.chunk_kda_bwd_state(d.q, d.k, d.v, d.g, d.beta, None, None, o, None),
              lambda: kda.recurrent_kda(d.q, d.k, d.v, d.g, d.beta), lambda: cp.compose(m, m, None)]
     torch.cuda.synchronize()
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)  # as if another GPU were the current one
+    current(monkeypatch, 1)  # as if another GPU were the current one
     for call in calls:
         with pytest.raises(ValueError, match="current device is cuda:1"):
             call()
