@@ -81,8 +81,8 @@ kda_status check_linear(const kda_linear *p, Linear &L) {
 }
 
 // What the clipping writes must not overlap: blocks would scale the shared elements
-// in no order. Addresses that ascend, as those of views of one buffer do, are
-// checked as they come; others are sorted (1 us for 100 tensors).
+// in no order. Addresses that ascend within a type, as those of views of one flat
+// buffer a type do, are checked as they come; others are sorted.
 struct Span {
   uintptr_t begin, end;
   int tensor;
@@ -92,15 +92,17 @@ kda_status check_outputs(int count, void *const *out, const int64_t *sizes, cons
     const uintptr_t p = (uintptr_t)out[i];
     return Span{p, p + (uintptr_t)sizes[i] * (dtypes[i] == KDA_BF16 ? 2 : 4), i};
   };
-  uintptr_t end = 0;
+  uintptr_t first[2] = {0, 0}, end[2] = {0, 0};  // of each type
   int i = 0;
   for (; i < count; ++i) {
     if (sizes[i] == 0) continue;
     const Span s = span(i);
-    if (s.begin < end) break;
-    end = s.end;
+    const int t = dtypes[i] == KDA_BF16;
+    if (s.begin < end[t]) break;
+    if (end[t] == 0) first[t] = s.begin;
+    end[t] = s.end;
   }
-  if (i == count) return KDA_OK;
+  if (i == count && (end[0] <= first[1] || end[1] <= first[0])) return KDA_OK;
   const std::unique_ptr<Span[]> all(new (std::nothrow) Span[count]);
   if (all == nullptr) return fail(KDA_ERR_UNSUPPORTED, "clip: no host memory for %d tensors", count);
   int n = 0;

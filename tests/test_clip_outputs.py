@@ -27,6 +27,8 @@ def clip(lib, at, sizes, kinds):
     ([A + 100, A, A + 40], [4, 11, 4], [0, 0, 0]),
     ([A, A + 4], [3, 4], [1, 0]),                              # bf16 and fp32
     ([A, A + 8], [100, 1], [0, 0]),                            # one inside the other
+    ([A, A + 64, A + 16, A + 80], [4, 4, 32, 4], [0, 1, 0, 1]),  # each type ascends, the two meet
+    ([A + 64, A, A + 80, A + 8], [4, 4, 4, 100], [0, 1, 0, 1]),
 ])
 def test_overlapping_outputs(lib, at, sizes, kinds):
     assert clip(lib, at, sizes, kinds) == _lib.KDA_ERR_INVALID_ARG
