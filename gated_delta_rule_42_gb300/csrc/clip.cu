@@ -8,9 +8,9 @@
 // kept between calls), cut into chunks of 8192 elements.  Each block has a
 // contiguous run of chunks, so that it searches the table once and then steps
 // along it.  The second pass gives the blocks the same runs, from the end: what the
-// first pass read last is still in L2.  1.34 G elements (2.7 GB of bf16): 417 us for
-// the norm (6.4 TB/s), 830 us for the scaling (6.5 TB/s).  With chunks of 4096, and
-// so half the loads in flight, the norm took 525 us.
+// first pass read last is still in L2.  1.34 G elements (2.7 GB of bf16): 405 us for
+// the norm (6.6 TB/s), 840 us for the scaling (6.4 TB/s).  With chunks of 4096, and
+// so half the loads in flight, the norm took 525 us (417 with 8192 at the time).
 #include "dense_internal.cuh"
 
 namespace kda {

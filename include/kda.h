@@ -241,11 +241,13 @@ kda_status kda_state_compose(const float *M, const float *h, const float *c, flo
                              int V, int transpose, void *stream);
 
 /* ---- the dense operators around the op in a training step ----
- * A KDA block is a layer norm, the projections that make q, k, v, the gate and
- * beta, the op, and an output projection added to the residual stream; its
- * training step ends with the clipping of the gradients' global norm.  These
- * entry points do that work on the same terms as the op: caller-owned buffers,
- * no allocation, no synchronisation, host-checkable errors before any launch.
+ * A block around the op has a norm, the projections that make q, k, v, the gate
+ * and beta, and an output projection added to the residual stream; its training
+ * step ends with the clipping of the gradients' global norm.  These entry points
+ * do that work, with a layer norm (the source pages' KDA layer has RMS norms, and
+ * a gated one at its output: not among them), on the same terms as the op:
+ * caller-owned buffers, no allocation of device memory, no synchronisation,
+ * host-checkable errors before any launch.
  * Every sum is held in fp32 or more and added in a fixed order: the same call
  * gives the same bits. */
 
