@@ -3,6 +3,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <cmath>
 #include <memory>
 #include <new>
 
@@ -82,12 +83,16 @@ kda_status check_linear(const kda_linear *p, Linear &L) {
 
 // What the clipping writes must not overlap: blocks would scale the shared elements
 // in no order. Addresses that ascend within a type, as those of views of one flat
-// buffer a type do, are checked as they come; others are sorted.
+// buffer a type do, are checked as they come; others are sorted. With an infinite
+// bound what is its own output is not written and does not count.
 struct Span {
   uintptr_t begin, end;
   int tensor;
 };
-kda_status check_outputs(int count, void *const *out, const int64_t *sizes, const int *dtypes) {
+kda_status check_outputs(int count, const void *const *in, void *const *out, const int64_t *sizes, const int *dtypes,
+                         float max_norm) {
+  const bool norm_alone = std::isinf(max_norm);
+  const auto written = [&](int i) { return sizes[i] != 0 && !(norm_alone && out[i] == in[i]); };
   const auto span = [&](int i) {
     const uintptr_t p = (uintptr_t)out[i];
     return Span{p, p + (uintptr_t)sizes[i] * (dtypes[i] == KDA_BF16 ? 2 : 4), i};
@@ -95,7 +100,7 @@ kda_status check_outputs(int count, void *const *out, const int64_t *sizes, cons
   uintptr_t first[2] = {0, 0}, end[2] = {0, 0};  // of each type
   int i = 0;
   for (; i < count; ++i) {
-    if (sizes[i] == 0) continue;
+    if (!written(i)) continue;
     const Span s = span(i);
     const int t = dtypes[i] == KDA_BF16;
     if (s.begin < end[t]) break;
@@ -107,7 +112,7 @@ kda_status check_outputs(int count, void *const *out, const int64_t *sizes, cons
   if (all == nullptr) return fail(KDA_ERR_UNSUPPORTED, "clip: no host memory for %d tensors", count);
   int n = 0;
   for (i = 0; i < count; ++i)
-    if (sizes[i] != 0) all[n++] = span(i);
+    if (written(i)) all[n++] = span(i);
   std::sort(all.get(), all.get() + n, [](const Span &a, const Span &b) {
     return a.begin != b.begin ? a.begin < b.begin : a.tensor < b.tensor;
   });
@@ -248,7 +253,7 @@ kda_status kda_clip_grad_norm(int count, const void *const *in, void *const *out
       return fail(KDA_ERR_INVALID_ARG, "clip: output %d is NULL or misaligned", i);
   }
   kda_status st = workspace_ok(workspace, workspace_bytes, clip_workspace(count));
-  if (st != KDA_OK || (out != nullptr && (st = check_outputs(count, out, sizes, dtypes)) != KDA_OK)) return st;
+  if (st != KDA_OK || (out != nullptr && (st = check_outputs(count, in, out, sizes, dtypes, max_norm)) != KDA_OK)) return st;
   return done(launch_clip(count, in, out, sizes, dtypes, max_norm, norm, static_cast<double *>(workspace),
                           (cudaStream_t)stream),
               "kda_clip_grad_norm");

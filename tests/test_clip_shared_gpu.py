@@ -40,6 +40,13 @@ def test_a_tensor_is_read_twice():
     assert all(torch.allclose(o, torch.full_like(o, 0.5)) for o in out)
 
 
+def test_the_norm_alone_of_a_tensor_listed_twice():
+    a = torch.ones(8, device="cuda")
+    assert float(kda.clip_grad_norm([a, a], math.inf)) == 4.0 and (a == 1).all()
+    with pytest.raises(RuntimeError, match="overlap"):  # here the outputs are written
+        kda.clip_grad_norm([a, a], math.inf, out=[torch.empty_like(a)] * 2)
+
+
 def test_empty_tensors_may_share_an_address():
     e = torch.empty(0, device="cuda")
     t = torch.ones(4, device="cuda")
