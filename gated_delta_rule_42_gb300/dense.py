@@ -28,7 +28,7 @@ __all__ = ["layer_norm", "layer_norm_fwd", "layer_norm_bwd", "linear", "linear_f
 
 _DTYPE = {torch.float32: _lib.KDA_F32, torch.bfloat16: _lib.KDA_BF16}
 _dtype_of = attrgetter("dtype")
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _SIZE_MAX = ctypes.c_size_t(-1).value
 _ACT = {None: 0, "silu": 1, "gelu": 2, "sigmoid": 3}
 

@@ -114,7 +114,7 @@ def make_inputs_struct(q, k, v, g, beta, initial_state=None, cu_seqlens=None, us
     return s
 
 
-_current_device = torch._C._cuda_getDevice
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # a torch without CUDA has none
 
 
 def _refuse_device(device):

@@ -334,9 +334,10 @@ kda_status kda_linear_status(int **word);
  * otherwise not overlap any input; written outputs that overlap are refused.
  * The squares are summed in fp32 over up to 32 elements and in fp64 beyond;
  * elements whose squares lie outside fp32 are scaled first, so that the norm is
- * accurate over the whole range of the types.  An infinite element scales by 0 and a NaN by NaN, as the formula has it: read
- * *norm to skip the step.  max_norm >= 0 and not NaN; an infinite max_norm scales
- * nothing; at most 2^42 elements in all.  The workspace is 256-byte aligned. */
+ * accurate over the whole range of the types.  An infinite element scales by 0
+ * and a NaN by NaN, as the formula has it: read *norm to skip the step.  max_norm
+ * >= 0 and not NaN; an infinite max_norm scales nothing; at most 2^42 elements in
+ * all.  The workspace is 256-byte aligned. */
 size_t kda_clip_grad_norm_workspace_size(int count);
 kda_status kda_clip_grad_norm(int count, const void *const *in, void *const *out, const int64_t *sizes,
                               const int *dtypes, float max_norm, float *norm, void *workspace,

@@ -1,5 +1,9 @@
 """Tensors of a device that is not the current one are refused before any launch: their
 addresses and their stream's handle mean nothing on the device that would run the kernels."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -44,3 +48,11 @@ def test_every_call_refuses(monkeypatch):
             call()
     monkeypatch.undo()
     assert (x == 1).all() and all(c() is not None for c in calls[:7])
+
+
+def test_the_package_loads_with_a_torch_without_cuda():
+    code = ("import torch; del torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream; "
+            "import gated_delta_rule_42_gb300.cp")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
